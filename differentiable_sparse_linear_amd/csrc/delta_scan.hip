@@ -80,9 +80,8 @@ struct StateOrder {
 };
 template <int NP, int DK>
 struct OutputOrder {
-    static constexpr int PP = NP == 3 ? 3 : 2;             // planes that reach the output
     static constexpr int KB = DK / 32;
-    static constexpr int kSince = KB * NP, kP = kSince + 1, kTotal = kP + 2 * PP;
+    static constexpr int kSince = KB * NP, kP = kSince + 1, kTotal = kP + 6;
     static constexpr int D = kTotal, N = kTotal;
 };
 
@@ -95,11 +94,11 @@ delta_scan_kernel(DeltaArgs a, ChunkRange cr, const unsigned char *ws_key,
     using L = PrepLayout<NP, DK>;
     using Y = OutputOrder<NP, DK>;
     using Z = StateOrder<NP, DK>;
-    constexpr int KB = Z::KB, TW = Z::TW, PP = Y::PP, KT = DK / 16;
+    constexpr int KB = Z::KB, TW = Z::TW, KT = DK / 16;
     __shared__ Shared<3, KB> Sx[NC];   // S
     __shared__ Shared<3, 2> Rx[NC];    // R
     __shared__ Shared<3, 2> Ux[NC];    // until beta W
-    __shared__ Shared<PP, 2> Wx[NC];   // W, for the output
+    __shared__ Shared<3, 2> Wx[NC];    // W, for the output
     int b, h, part;
     if (!head_and_part(a, b, h, part)) return;
     const int hk = h / (a.Hv / a.Hk), len = seq_len(a, b), live = live_chunks(cr, len);
@@ -110,7 +109,6 @@ delta_scan_kernel(DeltaArgs a, ChunkRange cr, const unsigned char *ws_key,
     const uint32_t lane16 = 16 * l;
     using Inputs = std::integral_constant<int, NP>;
     using Three = std::integral_constant<int, 3>;
-    using Out = std::integral_constant<int, PP>;
 
     // this chunk's workspace and the next one's; a head's chunks follow one another
     const unsigned char *key_at = ws_key + cr.key_chunk(a, b, hk, 0) * L::kPerKeyHead,
@@ -133,7 +131,9 @@ delta_scan_kernel(DeltaArgs a, ChunkRange cr, const unsigned char *ws_key,
         return load16(key, k_lane, base + (j / NP * 4 * NP + j % NP) * 1024);
     };
 
-    if (wave >= 4) {  // o = scale (Gamma Q S + P' W)
+    // o = scale (Gamma Q S + P' W), to 24 bits for every type: the two parts cancel
+    // where a token reads what it has just corrected
+    if (wave >= 4) {
         T *oc = o + b * ob + h * oh + col0;
         Rows<T> o_rows[NC];  // of this wavefront's tokens; lanes past the columns reach nothing
 #pragma unroll
@@ -143,7 +143,7 @@ delta_scan_kernel(DeltaArgs a, ChunkRange cr, const unsigned char *ws_key,
             if (j < Y::kSince) return rows_of_key(key, L::kKey + L::kKeyT, j);
             if (j == Y::kSince) return load16(head, s_lane, 2 * L::kTri);
             return load16(head, x_lane,
-                          L::kTri + ((j - Y::kP) % PP * kTriTiles + (j - Y::kP) / PP) * 1024);
+                          L::kTri + ((j - Y::kP) % 3 * kTriTiles + (j - Y::kP) / 3) * 1024);
         };
         Ring<Y::N, Y::D> ring;
         auto frag = [&](auto n, int j) {
@@ -164,7 +164,7 @@ delta_scan_kernel(DeltaArgs a, ChunkRange cr, const unsigned char *ws_key,
             for (int kb = 0; kb < KB; ++kb) {
                 const Frag<NP> q = frag(Inputs{}, kb * NP);
 #pragma unroll
-                for (int m = 0; m < NC; ++m) O[m] = mac<PP - 1>(q, Sx[m].get(kb, l), O[m]);
+                for (int m = 0; m < NC; ++m) O[m] = mac(q, Sx[m].get(kb, l), O[m]);
                 ring.next(kb * NP, NP, fetch);
             }
             const f32x4 since = __builtin_bit_cast(f32x4, ring.at(Y::kSince));
@@ -173,14 +173,14 @@ delta_scan_kernel(DeltaArgs a, ChunkRange cr, const unsigned char *ws_key,
             ring.next(Y::kSince, 1, fetch);
             exchange();
             exchange();  // W is there
-            const Frag<PP> p0 = frag(Out{}, Y::kP), p1 = frag(Out{}, Y::kP + PP);
+            const Frag<3> p0 = frag(Three{}, Y::kP), p1 = frag(Three{}, Y::kP + 3);
             const Buffer dst = Rows<T>::chunk(oc + t0 * ot, ot, a.T - t0);
 #pragma unroll
             for (int m = 0; m < NC; ++m) {
-                O[m] = mac<PP - 1>(p0, Wx[m].get(0, l), O[m]);
-                if (w >= 2) O[m] = mac<PP - 1>(p1, Wx[m].get(1, l), O[m]);
+                O[m] = mac(p0, Wx[m].get(0, l), O[m]);
+                if (w >= 2) O[m] = mac(p1, Wx[m].get(1, l), O[m]);
             }
-            ring.next(Y::kP, 2 * PP, fetch);
+            ring.next(Y::kP, 6, fetch);
 #pragma unroll
             for (int m = 0; m < NC; ++m)
 #pragma unroll

@@ -85,11 +85,11 @@ __device__ inline f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// c + a b, the plane pairs (i, j) with i + j <= ORD: 24 bits for 2, 16 for 1.
-template <int ORD = 2, int NA, int NB>
+// c + a b, the plane pairs (i, j) with i + j <= 2: 24 bits.
+template <int NA, int NB>
 __device__ inline f32x4 mac(const Frag<NA> &a, const Frag<NB> &b, f32x4 c) {
 #pragma unroll
-    for (int s = ORD; s >= 0; --s)
+    for (int s = 2; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
             if (s - i >= 0 && s - i < NB) c = mfma(a.p[i], b.p[s - i], c);
@@ -98,11 +98,11 @@ __device__ inline f32x4 mac(const Frag<NA> &a, const Frag<NB> &b, f32x4 c) {
 
 // c0 + a0 b0 and c1 + a1 b1, their steps in turn: a step waits for the one
 // before it in its own sum.
-template <int ORD = 2, int NA, int NB>
+template <int NA, int NB>
 __device__ inline void mac_pair(const Frag<NA> &a0, const Frag<NB> &b0, f32x4 &c0,
                                 const Frag<NA> &a1, const Frag<NB> &b1, f32x4 &c1) {
 #pragma unroll
-    for (int s = ORD; s >= 0; --s)
+    for (int s = 2; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
             if (s - i >= 0 && s - i < NB) {
