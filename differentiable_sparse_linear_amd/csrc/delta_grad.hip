@@ -14,10 +14,16 @@ namespace {
 //   h_j     = until_j dS w_j + sum_i (y_ij k_i + z_ij q~_i)   (k wrote it)
 //   dbeta_j = k_j . h_j
 //
-// and for G, the running sum of gates, dG_i = q~_i . dq~_i + k_i . r_i -
-// beta_i dbeta_i, with <S', dS> of the chunk's end (S' the state there)
-//   exp(G_C) <S, dS> + sum_j beta_j until_j k_j . dS w_j
-// added to the last one; dgate is its sum from the token to the chunk's end.
+// A gate acts on everything that passes its token t:
+//
+//   dgate_t = sum_(i >= t) A_i + sum_(j < t) B_j + sum_(j < t <= i) E_ij + exp(G_C) <S, dS>
+//     A_i  = Gamma_i (q~_i . S dO_i - k_i . S dR_i)
+//     B_j  = beta_j until_j k_j . dS w_j
+//     E_ij = beta_j (z_ij q~_i . k_j + y_ij k_i . k_j)
+//
+// Each term has a_t as a factor, so a strong decay's gradient is as exact as a weak
+// one's.  (As the sum of q~_i . dq~_i + k_i . r_i - beta_i dbeta_i from t on it would
+// be a difference of terms that have not.)
 //
 // One workgroup takes one chunk of one key head and sums over the value
 // heads that share it, so no sum depends on the order of workgroups.  Wavefront
@@ -33,11 +39,11 @@ namespace {
 // (1024 threads, 128 registers) spill: 142 and 85.  A double stage: 104 and 83.
 template <typename T, int DK, bool GROUP>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void
-delta_grad_kernel(DeltaArgs a, ChunkRange cr, bool vec_o, const unsigned char *ws_key,
+delta_grad_kernel(DeltaArgs a, ChunkRange cr, bool vec_q, bool vec_o, const unsigned char *ws_key,
                   const unsigned char *ws_head, const T *grad_o, int64_t ob, int64_t ot,
                   int64_t oh, T *dq, T *dk, float *dbeta, float *dgate, const float *save_s,
                   const float *save_w, const float *ws_ds, const float *ws_dr) {
-    constexpr int NP = Planes<T>::n, KT = DK / 16, HT = KT / 2, LD = 68;
+    constexpr int NP = Planes<T>::n, KT = DK / 16, HT = KT / 2, KB = DK / 32, LD = 68;
     constexpr int kThreads = 512;
     using L = PrepLayout<NP, DK>;
     const int n = cr.first + blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
@@ -68,7 +74,8 @@ delta_grad_kernel(DeltaArgs a, ChunkRange cr, bool vec_o, const unsigned char *w
     constexpr int kStage = 2 * kStateBytes + 2 * kRowBytes, kTri = 2 * 64 * LD * 4;
     __shared__ __align__(16) unsigned char lds[kStage > kTri ? kStage : kTri];
     __shared__ double Gs[64];
-    __shared__ float Bs[64], dots[2][3][64];
+    __shared__ float Bs[64], dots[2][4][64];    // of a token: A, dbeta, B, its rows' E
+    __shared__ float below[2][4][64], ends[8];  // E's sums over a row tile; <S, dS>
     unsigned char *Sp = lds, *Dp = lds + kStateBytes, *Wp = lds + 2 * kStateBytes,
                   *Rp = Wp + kRowBytes;
     float *Zb = reinterpret_cast<float *>(lds), *Yb = Zb + 64 * LD;
@@ -172,23 +179,63 @@ delta_grad_kernel(DeltaArgs a, ChunkRange cr, bool vec_o, const unsigned char *w
         }
         const int tl = t0 + l;
         const float be = tl < len ? a.beta[b * a.bb + tl * a.bt + h * a.bh] : 0.f;
-        const float gate_l = tl < len ? a.gate[b * a.gb + tl * a.gt + h * a.gh] : 0.f;
         if (wave == 0) {
-            Gs[l] = gate_sum(gate_l, l);
+            Gs[l] = gate_sum(tl < len ? a.gate[b * a.gb + tl * a.gt + h * a.gh] : 0.f, l);
             Bs[l] = be;
         }
         exchange();
+        // q (half 0) or k (half 1) of this wavefront's tokens, for E
+        Frag<NP> xf[KB];
+        if (half) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    xf[kb].p[p] = load16(kq, lane16 + w * NP * 1024, (kb * 4 * NP + p) * 1024);
+        } else {
+            const int t = t0 + 16 * w + c;
+            const T *x = reinterpret_cast<const T *>(a.q) + b * a.qb + t * a.qt + hk * a.qh;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+                xf[kb] = load_frag<T>(x, 32 * kb + 4 * g, a.dk, t < len, vec_q);
+        }
+        float f[4] = {0.f, 0.f, 0.f, 0.f};  // of rows t: E_ij of j < t <= i, i in this tile
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int col = 16 * j + c;
+            f32x4 e = zero;
+            if (j <= w) {
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    Frag<NP> kf;
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        kf.p[p] = load16(kq, lane16, ((kb * 4 + j) * NP + p) * 1024);
+                    e = mac(xf[kb], kf, e);
+                }
+                e *= half ? Bs[col] : a.scale * Bs[col];
+            }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = 16 * w + 4 * g + r, col = 16 * j + c;
+                const int row = 16 * w + 4 * g + r;
                 const float D = row >= col ? decay(Gs[row] - Gs[col]) : 0.f;
-                if (half)
-                    Yb[row * LD + col] = row > col ? -D * zy[j][r] : 0.f;
-                else
-                    Zb[row * LD + col] = D * zy[j][r];
+                const float y = half ? row > col ? -D * zy[j][r] : 0.f : D * zy[j][r];
+                (half ? Yb : Zb)[row * LD + col] = y;
+                e[r] = row > col ? e[r] * y : 0.f;
             }
+            // sums from a row to the tile's end
+#pragma unroll
+            for (int r = 2; r >= 0; --r) e[r] += e[r + 1];
+            float later = 0.f;
+#pragma unroll
+            for (int d = 1; d < 4; ++d) {
+                const float y = __shfl_down(e[0], 16 * d, 64);
+                later += g + d < 4 ? y : 0.f;
+            }
+            if (g == 0) below[half][w][col] = e[0] + later;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) f[r] += 16 * w + 4 * g + r > col ? e[r] + later : 0.f;
+        }
         const f32x4 since = *reinterpret_cast<const f32x4 *>(scalars + 16 * w + 4 * g);
         const f32x4 until = *reinterpret_cast<const f32x4 *>(scalars + 64 + 16 * w + 4 * g);
         const f32x4 beta = *reinterpret_cast<const f32x4 *>(scalars + 128 + 16 * w + 4 * g);
@@ -214,15 +261,27 @@ delta_grad_kernel(DeltaArgs a, ChunkRange cr, bool vec_o, const unsigned char *w
             kv[t] = values(f, w & 1);
             qv[t] = values(q, w & 1) * a.scale;
         }
-        // the parts of <S', dS>: S's, and beta_j k_j . (until_j dS w_j)
-        inner *= scalars[63];
+        // A and B, before the pairs' terms come to aq, ar and hh
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            float y = 0.f;
+            float A = 0.f, B = 0.f;
 #pragma unroll
-            for (int i = 0; i < HT; ++i) y = fmaf(kv[i][r], hh[i][r], y);
-            inner = fmaf(beta[r], y, inner);
+            for (int i = 0; i < HT; ++i) {
+                A = fmaf(qv[i][r], aq[i][r], fmaf(kv[i][r], ar[i][r], A));
+                B = fmaf(kv[i][r], hh[i][r], B);
+            }
+            A = sum16(A), B = sum16(beta[r] * B);
+            const float F = sum16(f[r]);
+            if (c == 0) {
+                dots[half][0][16 * w + 4 * g + r] = A;
+                dots[half][2][16 * w + 4 * g + r] = B;
+                dots[half][3][16 * w + 4 * g + r] = F;
+            }
         }
+        inner *= scalars[63];
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) inner += __shfl_xor(inner, off, 64);
+        if (l == 0) ends[wave] = inner;
         exchange();
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
@@ -268,45 +327,44 @@ delta_grad_kernel(DeltaArgs a, ChunkRange cr, bool vec_o, const unsigned char *w
                 }
             }
         }
-        // rows 4 g + r of this wavefront's 16 tokens: the dots with q and k
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            float dG = 0.f, db = 0.f;
+            float db = 0.f;
 #pragma unroll
-            for (int i = 0; i < HT; ++i) {
-                dG = fmaf(qv[i][r], aq[i][r], fmaf(kv[i][r], ar[i][r], dG));
-                db = fmaf(kv[i][r], hh[i][r], db);
-            }
-#pragma unroll
-            for (int off = 1; off < 16; off <<= 1) {
-                dG += __shfl_xor(dG, off, 64);
-                db += __shfl_xor(db, off, 64);
-            }
-            if (c == 0) {
-                dots[half][0][16 * w + 4 * g + r] = dG;
-                dots[half][1][16 * w + 4 * g + r] = db;
-            }
+            for (int i = 0; i < HT; ++i) db = fmaf(kv[i][r], hh[i][r], db);
+            db = sum16(db);
+            if (c == 0) dots[half][1][16 * w + 4 * g + r] = db;
         }
-        dots[half][2][16 * w + c] = 0.f;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) inner += __shfl_xor(inner, off, 64);
-        if (l == 0) dots[half][2][16 * w] = inner;
         exchange();
-        if (wave == 0) {
-            const float db = dots[0][1][l] + dots[1][1][l];
-            float dG = dots[0][0][l] + dots[1][0][l] - be * db, end = dots[0][2][l] + dots[1][2][l];
+        if (wave == 0) {  // lane t
+            float A = dots[0][0][l] + dots[1][0][l], B = dots[0][2][l] + dots[1][2][l],
+                  dg = dots[0][3][l] + dots[1][3][l], end = 0.f, past[3];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) end += ends[i];
+            // past[i]: of rows beyond tile i, then of columns up to this lane's
+#pragma unroll
+            for (int i = 2; i >= 0; --i)
+                past[i] = (i < 2 ? past[i + 1] : 0.f) + below[0][i + 1][l] + below[1][i + 1][l];
 #pragma unroll
             for (int off = 1; off < 64; off <<= 1) {
-                const float up = __shfl_down(dG, off, 64);
-                if (l + off < 64) dG += up;
-                end += __shfl_xor(end, off, 64);
+                const float later = __shfl_down(A, off, 64), earlier = __shfl_up(B, off, 64);
+                A += l + off < 64 ? later : 0.f;
+                B += l >= off ? earlier : 0.f;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const float y = __shfl_up(past[i], off, 64);
+                    past[i] += l >= off ? y : 0.f;
+                }
             }
+            B = __shfl_up(B, 1, 64);  // of tokens before this one
+#pragma unroll
+            for (int i = 0; i < 3; ++i) past[i] = __shfl_up(past[i], 1, 64);
+            dg += A + end + (l > 0 ? B : 0.f) +
+                  (l >= 48 || l == 0 ? 0.f : l >= 32 ? past[2] : l >= 16 ? past[1] : past[0]);
             if (tl < a.T) {
                 const int64_t out = ((int64_t)b * a.T + tl) * a.Hv + h;
-                const bool in = tl < len;
-                dbeta[out] = in ? db : 0.f;
-                // where the gate erased the state, it has no gradient
-                dgate[out] = in && expf(gate_l) != 0.f ? dG + end : 0.f;
+                dbeta[out] = tl < len ? dots[0][1][l] + dots[1][1][l] : 0.f;
+                dgate[out] = tl < len ? dg : 0.f;
             }
         }
 #pragma unroll
@@ -346,7 +404,7 @@ hipError_t grad_t(const DeltaArgs &a, const ChunkRange &cr, const DeltaBackward 
     const dim3 grid(cr.count, a.Hk, a.B);
     auto kernel = a.Hv > a.Hk ? delta_grad_kernel<T, DK, true> : delta_grad_kernel<T, DK, false>;
     kernel<<<grid, 512, 0, s>>>(
-        a, cr, vec_o, ws_key, ws_head, reinterpret_cast<const T *>(f.grad_o), f.ob, f.ot, f.oh,
+        a, cr, rows_aligned(a, sizeof(T)), vec_o, ws_key, ws_head, reinterpret_cast<const T *>(f.grad_o), f.ob, f.ot, f.oh,
         reinterpret_cast<T *>(f.dq), reinterpret_cast<T *>(f.dk), f.dbeta, f.dgate, f.save_s,
         f.save_w, f.ws_ds, f.ws_dr);
     return hipGetLastError();

@@ -16,6 +16,8 @@
 // stand: results feed the next product without leaving their lane.
 #pragma once
 
+#include <type_traits>
+
 #include "delta.h"
 
 namespace sla {
@@ -340,6 +342,19 @@ __device__ inline Frag<Planes<T>::n> row_frag(Buffer b, uint32_t at, int left, b
         for (int e = 0; e < 8; ++e) y[e] = to_f32<T>(x[e]);
         return split<Planes<T>::n>(y);
     }
+}
+
+// The sum over the 16 lanes that share g, in each of them.
+__device__ inline float sum16(float x) {
+    auto add = [&](auto ror) {
+        x += __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(x),
+                                                         0x120 + decltype(ror)::value, 0xf, 0xf, false));
+    };
+    add(std::integral_constant<int, 8>{});
+    add(std::integral_constant<int, 4>{});
+    add(std::integral_constant<int, 2>{});
+    add(std::integral_constant<int, 1>{});
+    return x;
 }
 
 // A barrier for exchanges through LDS: what was put there is there, what was

@@ -52,3 +52,56 @@ def test_output_where_a_token_reads_what_it_corrects(hip, dtype, save, size):
     off, bound = norms(o.double() - want), ROUND[dtype] * norms(want) + 8e-7 * norms(terms)
     print("off", off.tolist(), "bound", bound.tolist())
     assert (off <= bound).all()
+
+
+def walk(q, k, v, beta, gate, grad_o, grad_state, scale):
+    """Per head, the largest of ||S_t|| and |v_t|, and of ||dS_t|| and |dO_t|."""
+    group = v.shape[2] // q.shape[2]
+    q, k = (x.double().repeat_interleave(group, dim=2) for x in (q, k))
+    v, beta, a, do = v.double(), beta.double(), gate.double().exp(), grad_o.double()
+    top, dtop = v.norm(dim=-1).amax(1), do.norm(dim=-1).amax(1)
+    S = torch.zeros_like(grad_state, dtype=torch.float64)
+    dS = grad_state.double()
+    for t in range(v.shape[1]):
+        S = a[:, t, :, None, None] * S
+        w = v[:, t] - (S * k[:, t, :, :, None]).sum(2)
+        S = S + k[:, t, :, :, None] * (beta[:, t, :, None] * w)[:, :, None, :]
+        top = torch.maximum(top, S.norm(dim=(2, 3)))
+    for t in reversed(range(v.shape[1])):
+        dS = dS + scale * q[:, t, :, :, None] * do[:, t, :, None, :]
+        dtop = torch.maximum(dtop, dS.norm(dim=(2, 3)))
+        dw = beta[:, t, :, None] * (dS * k[:, t, :, :, None]).sum(2)
+        dS = a[:, t, :, None, None] * (dS - k[:, t, :, :, None] * dw[:, :, None, :])
+    return top, dtop
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("T,Hk,Hv,dk,dv", [(60, 1, 2, 40, 48), (150, 2, 4, 128, 64), (130, 2, 2, 64, 33)])
+def test_gate_gradients_of_strong_decays(hip, dtype, T, Hk, Hv, dk, dv):
+    """Every token's own gradient where strong decays stand among weak ones.
+
+    The gate's gradient is a_t <dS, S_(t-1)> (after and before the token): a_t times
+    inner products of what the passes carry, each good to 1.5e-6 for a chunk, the
+    two passes together twice that.  A difference of sums that lack a_t would be
+    off by 1e-7 of their size, for a gate of -20 the gradient's size 50 times."""
+    banner(f"gate gradients {dtype} {T} {Hk} {Hv} {dk} {dv}")
+    g = torch.Generator(device=DEV).manual_seed(22)
+    randn = lambda *s: torch.randn(s, generator=g, device=DEV)
+    B, norm = 2, torch.nn.functional.normalize
+    c = dict(q=norm(randn(B, T, Hk, dk), dim=-1).to(dtype), k=norm(randn(B, T, Hk, dk), dim=-1).to(dtype),
+             v=randn(B, T, Hv, dv).to(dtype), beta=torch.sigmoid(randn(B, T, Hv)),
+             gate=-0.1 * randn(B, T, Hv).abs())
+    strong = torch.tensor([-8.0, -12.0, -16.0, -20.0], device=DEV)
+    pick = torch.randint(0, 24, (B, T, Hv), generator=g, device=DEV)
+    c["gate"] = torch.where(pick < 4, strong[pick.clamp(max=3)], c["gate"])
+    c["gate"][0, :, 0] = -16.0          # and a head of strong decays alone
+    go, gs = randn(B, T, Hv, dv).to(dtype), randn(B, Hv, dk, dv)
+    gate = c["gate"].clone().requires_grad_()
+    o, S = hip.delta_rule(**{**c, "gate": gate}, scale=1.0)
+    (got,) = torch.autograd.grad([o, S], gate, [go, gs])
+    want = OD.rule_adjoint(**c, grad_o=go, grad_state=gs, scale=1.0)["gate"]
+    top, dtop = walk(**c, grad_o=go, grad_state=gs, scale=1.0)
+    bound = 2 * 1.5e-6 * (T // 64 + 2) * c["gate"].double().exp() * (top * dtop)[:, None]
+    off = (got.double() - want).abs()
+    print("off / bound", float((off / bound).max()), "strong", float((off / bound)[pick < 4].max()))
+    assert (off <= bound).all()
