@@ -38,6 +38,13 @@ constexpr int kMaxDk = 128;      // largest key size: state rows held by one wav
 constexpr int kSlice = 16;       // state columns of one wavefront of the chunk scans
 constexpr float kMinGate = -1000.f;  // exp underflows to 0 far above: -inf acts like this
 
+// Whole sequences answer NaN where a run of gates within a chunk sums to more
+// than this.  A chunk's products hold decays between any two of its tokens, and
+// where tokens correct what grew between them (equal unit keys, beta = 1) the
+// grown terms cancel: a run of 2 loses a factor of 3 in accuracy, of 8 a factor
+// of 300, and 64 gates of 1 all digits.
+constexpr float kMaxGrowth = 2.f;
+
 // What every kernel of the rule reads; strides in elements, the last
 // dimension of each array contiguous.
 struct DeltaArgs {
@@ -81,6 +88,6 @@ __device__ inline __hip_bfloat16 from_f32<__hip_bfloat16>(float x) {
 
 hipError_t launch_delta_step(int dtype, const DeltaArgs &a, const float *s_in, float *s_out,
                              const int32_t *slots, int64_t n_slots, void *o, int64_t ob,
-                             int64_t ot, int64_t oh, hipStream_t s);
+                             int64_t ot, int64_t oh, float max_growth, hipStream_t s);
 
 }  // namespace sla

@@ -1,5 +1,7 @@
 // C entry points of the gated delta rule: argument checks, the workspace's
 // layout, and the rounds of launches.
+#include <cmath>
+
 #include "delta_chunk.h"
 
 namespace sla {
@@ -150,7 +152,7 @@ sla_status sla_delta_forward(const sla_delta_args *args, const float *d_state_in
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     if (!d_saved && few_tokens(a)) {
         DELTA_TRY(launch_delta_step(dtype, a, d_state_in, d_state_out, nullptr, 0, d_o, o_stride[0],
-                                    o_stride[1], o_stride[2], s));
+                                    o_stride[1], o_stride[2], kMaxGrowth, s));
         return SLA_OK;
     }
     const Work w = layout(a, dtype, false);
@@ -224,7 +226,7 @@ sla_status sla_delta_step(const sla_delta_args *args, float *d_state, int64_t n_
     if (args->batch == 0 || args->tokens == 0) return SLA_OK;
     if (!d_state || !d_o) return SLA_ERR_ARG;
     DELTA_TRY(launch_delta_step(args->dtype, args_of(args), d_state, d_state, d_slots, n_slots, d_o,
-                                o_stride[0], o_stride[1], o_stride[2],
+                                o_stride[0], o_stride[1], o_stride[2], HUGE_VALF,
                                 reinterpret_cast<hipStream_t>(stream)));
     return SLA_OK;
 }

@@ -16,6 +16,7 @@ struct StepArgs {
     int64_t n_slots;
     void *o;
     int64_t ob, ot, oh;
+    float max_growth;  // of a run of gates: kMaxGrowth or infinity
 };
 
 // One workgroup holds CL * VEC columns of one head's state in registers:
@@ -74,7 +75,7 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(StepArgs p) {
         if (d >= a.dk) return 0.f;
         return tid < kMaxDk ? to_f32<T>(k[t * a.kt + d]) : to_f32<T>(q[t * a.qt + d]);
     };
-    float next = len > 0 ? fetch(0) : 0.f;
+    float next = len > 0 ? fetch(0) : 0.f, run = 0.f;
     for (int t = 0; t < len; ++t) {
         float(*x)[2] = kq[t & 1];
         x[d][tid / kMaxDk] = next;
@@ -82,7 +83,9 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(StepArgs p) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
             vt[e] = col + e < a.dv ? to_f32<T>(v[t * a.vt + col + e]) : 0.f;
-        const float bt = beta[t * a.bt], at = expf(gate[t * a.gt]);
+        const float bt = beta[t * a.bt], gt = gate[t * a.gt];
+        run = fmaxf(run, 0.f) + gt;
+        const float at = run > p.max_growth ? __builtin_nanf("") : expf(gt);
         __syncthreads();
         if (t + 1 < len) next = fetch(t + 1);
         float sk[VEC] = {}, sq[VEC] = {}, dot = 0.f;
@@ -186,8 +189,8 @@ hipError_t launch_t(const StepArgs &p, hipStream_t s) {
 
 hipError_t launch_delta_step(int dtype, const DeltaArgs &a, const float *s_in, float *s_out,
                              const int32_t *slots, int64_t n_slots, void *o, int64_t ob,
-                             int64_t ot, int64_t oh, hipStream_t s) {
-    const StepArgs p{a, s_in, s_out, slots, n_slots, o, ob, ot, oh};
+                             int64_t ot, int64_t oh, float max_growth, hipStream_t s) {
+    const StepArgs p{a, s_in, s_out, slots, n_slots, o, ob, ot, oh, max_growth};
     return dtype == SLA_F32   ? launch_t<float>(p, s)
            : dtype == SLA_F16 ? launch_t<__half>(p, s)
                               : launch_t<__hip_bfloat16>(p, s);

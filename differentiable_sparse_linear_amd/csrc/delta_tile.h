@@ -375,7 +375,8 @@ __host__ __device__ constexpr int upper_tile(int i, int kb) {
 }
 
 // Gates of a chunk, one token a lane: the running sum in 64 bits and units of
-// log 2 (differences keep 32 bits whatever was summed before them).
+// log 2 (differences keep 32 bits whatever was summed before them); NaN where
+// the gates of a run of tokens sum to more than kMaxGrowth.
 __device__ inline double gate_sum(float gate, int lane) {
     double x = (gate < kMinGate ? kMinGate : gate) * kLog2e;
 #pragma unroll
@@ -383,7 +384,14 @@ __device__ inline double gate_sum(float gate, int lane) {
         const double y = __shfl_up(x, off, 64);
         if (lane >= off) x += y;
     }
-    return x;
+    float low = fminf((float)x, 0.f);  // the least sum up to here
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const float y = __shfl_up(low, off, 64);
+        if (lane >= off) low = fminf(low, y);
+    }
+    const bool grows = (float)x - low > (float)(kMaxGrowth * kLog2e);
+    return __any(grows) ? (double)__builtin_nanf("") : x;
 }
 
 // What the preparation of a chunk leaves for the scans and the gradients, in

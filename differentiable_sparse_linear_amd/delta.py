@@ -226,10 +226,12 @@ def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Te
     the decay) [batch, tokens, value heads] float32; state [batch, value
     heads, dk, dv] float32, zero by default; scale dk ** -0.5 by default;
     lengths [batch] int32: the tokens of each sequence that are in use (the
-    others are not read into any result and answer 0).  Differentiable in q,
-    k, v, beta, gate and state, once.  Workspaces and outputs come from
-    torch's allocator on the stream that the call runs on (``stream``, or the
-    current one)."""
+    others are not read into any result and answer 0).  Gates are logs of
+    decays, 0 or less: where the gates of a run of tokens within a chunk sum to
+    more than 2, or one is NaN, the head answers NaN from there on (and may from
+    the chunk's first token).  Differentiable in q, k, v, beta, gate and state,
+    once.  Workspaces and outputs come from torch's allocator on the stream that
+    the call runs on (``stream``, or the current one)."""
     device = _check_rule(q, k, v, beta, gate, state, lengths, 2)
     scale = q.shape[-1] ** -0.5 if scale is None else float(scale)
     with _on(device, stream):
@@ -248,7 +250,8 @@ def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: tor
     dv], beta, gate [batch, value heads]; state [slots, value heads, dk, dv]
     float32, contiguous: a pool, of which sequence b owns state[slots[b]]
     (slots int32, all different; without them state[b]).  A slot outside the
-    pool marks a place with no request: its o is 0.  No gradients."""
+    pool marks a place with no request: its o is 0.  Any gate is taken as the
+    formulas stand.  No gradients."""
     device = _check_rule(q, k, v, beta, gate, None, None, 1)
     vs, dk = v.shape, q.shape[-1]
     _need(state.dim() == 4, "state must have 4 dimensions")

@@ -360,8 +360,16 @@ enum { SLA_F16 = 2, SLA_BF16 = 3 };                /* tensor types, with SLA_F32
  * Every S is fp32; sums are taken in fp32 (of gates in fp64) and products
  * keep 24 bits, whatever the type of q, k, v and o.  A gate at or below
  * -104, -inf among them, erases the state (exp underflows to 0; the state must
- * be finite, 0 times infinity is NaN here as in the formula).  Gates above 0
- * and NaN give what the formulas give.
+ * be finite, 0 times infinity is NaN here as in the formula).
+ *
+ * Gates are logs of decays: 0 or less.  Whole sequences (sla_delta_forward and
+ * _backward) take them in chunks of 64 tokens and allow for growth as long as no
+ * run of gates within a chunk sums to more than 2; where one does, or a gate is
+ * NaN, the head's answers are NaN from there on, and may be from the chunk's
+ * first token.  A q, k, v or beta in use that is not finite makes answers NaN
+ * likewise: those of its head (of v: its column) from its chunk on.  Gradients
+ * of a head with such a token are NaN.  sla_delta_step takes any gate, token by
+ * token as the formulas stand.
  */
 typedef struct {
     int64_t batch, tokens;                   /* sequences; tokens of each (padded) */
