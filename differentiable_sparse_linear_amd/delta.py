@@ -180,14 +180,17 @@ def _forward(q, k, v, beta, gate, state, scale, lengths, save: bool):
 
 
 class DeltaRule(torch.autograd.Function):
-    """(o, last state); saves the inputs, the state at every chunk's start
-    and W (4 (dk / 64 + 1) dv bytes a token and value head, dk and dv padded
-    to whole tiles)."""
+    """(o, last state) of ``delta_rule``'s arguments, checked as there; saves
+    the inputs, the state at every chunk's start and W (4 (dk / 64 + 1) dv bytes
+    a token and value head, dk and dv padded to whole tiles)."""
 
     @staticmethod
     def forward(ctx, q, k, v, beta, gate, state, scale, lengths):
-        o, last, saved = _forward(q, k, v, beta, gate, state, scale, lengths,
-                                  any(ctx.needs_input_grad))
+        with _on(_check_rule(q, k, v, beta, gate, state, lengths, 2)):
+            q, k, v = _rows(q), _rows(k), _rows(v, tokens=True)
+            scale = q.shape[-1] ** -0.5 if scale is None else float(scale)
+            o, last, saved = _forward(q, k, v, beta, gate, state, scale, lengths,
+                                      any(ctx.needs_input_grad))
         if saved is not None:
             ctx.save_for_backward(q, k, v, beta, gate, lengths, saved)
             ctx.scale, ctx.has_state = scale, state is not None
@@ -232,12 +235,16 @@ def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Te
     the chunk's first token).  Differentiable in q, k, v, beta, gate and state,
     once.  Workspaces and outputs come from torch's allocator on the stream that
     the call runs on (``stream``, or the current one)."""
+    if torch.is_grad_enabled():
+        inputs = q, k, v, beta, gate, state, scale, lengths
+        if stream is None:
+            return DeltaRule.apply(*inputs)
+        with torch.cuda.stream(stream):
+            return DeltaRule.apply(*inputs)
     device = _check_rule(q, k, v, beta, gate, state, lengths, 2)
     scale = q.shape[-1] ** -0.5 if scale is None else float(scale)
     with _on(device, stream):
         q, k, v = _rows(q), _rows(k), _rows(v, tokens=True)
-        if torch.is_grad_enabled():
-            return DeltaRule.apply(q, k, v, beta, gate, state, scale, lengths)
         return _forward(q, k, v, beta, gate, state, scale, lengths, False)[:2]
 
 
