@@ -21,6 +21,7 @@ import struct
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import SLA_BF16, SLA_F16, SLA_F32, SLA_OK, SlaError, _on, _raw_stream, load
 
@@ -160,6 +161,17 @@ def _make_args(q, k, v, beta, gate, scale, lengths, tokens: bool = True) -> _Arg
     return args
 
 
+def _in_dual_level() -> bool:
+    """Whether tensors may carry forward-mode tangents (also with gradients off)."""
+    return forward_ad._current_level >= 0
+
+
+def _tracked(*xs) -> bool:
+    """Whether a derivative of a result by one of the tensors is asked for."""
+    return (torch.is_grad_enabled() and any(x.requires_grad for x in xs)) or (
+        _in_dual_level() and any(forward_ad.unpack_dual(x).tangent is not None for x in xs))
+
+
 def _bytes(n: int, device) -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
@@ -233,9 +245,9 @@ def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Te
     decays, 0 or less: where the gates of a run of tokens within a chunk sum to
     more than 2, or one is NaN, the head answers NaN from there on (and may from
     the chunk's first token).  Differentiable in q, k, v, beta, gate and state,
-    once.  Workspaces and outputs come from torch's allocator on the stream that
-    the call runs on (``stream``, or the current one)."""
-    if torch.is_grad_enabled():
+    once, in reverse mode.  Workspaces and outputs come from torch's allocator
+    on the stream that the call runs on (``stream``, or the current one)."""
+    if torch.is_grad_enabled() or _in_dual_level():
         inputs = q, k, v, beta, gate, state, scale, lengths
         if stream is None:
             return DeltaRule.apply(*inputs)
@@ -258,7 +270,8 @@ def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: tor
     float32, contiguous: a pool, of which sequence b owns state[slots[b]]
     (slots int32, all different; without them state[b]).  A slot outside the
     pool marks a place with no request: its o is 0.  Any gate is taken as the
-    formulas stand.  No gradients."""
+    formulas stand.  It has no derivatives and refuses tensors that ask for them
+    (under ``torch.no_grad()`` none does)."""
     device = _check_rule(q, k, v, beta, gate, None, None, 1)
     vs, dk = v.shape, q.shape[-1]
     _need(state.dim() == 4, "state must have 4 dimensions")
@@ -272,6 +285,9 @@ def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: tor
     if out is not None:
         _like(out, "out", vs, v.dtype, device)
         _need(vs[2] == 1 or out.stride(-1) == 1, "out's last dimension must be contiguous")
+    if _tracked(q, k, v, beta, gate, state, *(() if out is None else (out,))):
+        raise ValueError("delta_rule_step has no derivatives: call it under torch.no_grad(), "
+                         "or delta_rule on sequences of one token")
     scale = dk ** -0.5 if scale is None else float(scale)
     with _on(device, stream):
         q, k, v = _rows(q), _rows(k), _rows(v)

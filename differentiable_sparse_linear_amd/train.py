@@ -112,7 +112,7 @@ def grad_norm(grads: Iterable[torch.Tensor], stream=None) -> torch.Tensor:
     """The 2-norm of all the tensors together, a scalar on their device:
     float64 if one of them is, else float32 (squares and sums are taken in
     fp64).  Tensors of any mix of float64, float32, float16 and bfloat16,
-    contiguous."""
+    contiguous.  A number about them: no gradient flows through it."""
     grads = _tensors(grads)
     if not grads:
         return torch.zeros((), device="cuda")

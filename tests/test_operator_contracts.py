@@ -50,3 +50,41 @@ def test_function_takes_strided_rows(hip):
     ga = torch.autograd.grad(got[0].square().sum(), [wide["q"], wide["k"], wide["v"]])
     gb = torch.autograd.grad(want[0].square().sum(), [flat["q"], flat["k"], flat["v"]])
     assert all(torch.equal(a, b) for a, b in zip(ga, gb))
+
+
+# ------------------------------------------------------ derivatives not given
+
+@pytest.mark.gpu
+def test_forward_mode_is_refused_not_dropped(hip):
+    """A tangent is an error also with gradients off, where torch's own operations
+    carry it on."""
+    from torch.autograd import forward_ad
+    c = rule_inputs(DEV)
+    with forward_ad.dual_level():
+        dual = {**c, "v": forward_ad.make_dual(c["v"], torch.ones_like(c["v"]))}
+        for context in (torch.no_grad(), torch.enable_grad()):
+            with context, pytest.raises(NotImplementedError):
+                hip.delta_rule(**dual)
+        one = {n: x[:, 0] if n != "state" else x.clone() for n, x in dual.items()}
+        with torch.no_grad(), pytest.raises(ValueError, match="no derivatives"):
+            hip.delta_rule_step(**one)
+        with torch.no_grad():       # tensors without a tangent are answered
+            o, S = hip.delta_rule(**c)
+    wo, wS = hip.delta_rule(**c)
+    assert torch.equal(o, wo) and torch.equal(S, wS)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["q", "k", "v", "beta", "gate", "state"])
+def test_step_refuses_inputs_that_ask_for_gradients(hip, name):
+    c = rule_inputs(DEV)
+    one = {n: x[:, 0].clone() if n != "state" else x.clone() for n, x in c.items()}
+    with torch.no_grad():
+        want = hip.delta_rule_step(**{**one, "state": one["state"].clone()})
+    asks = {**one, name: one[name].requires_grad_()}
+    before = asks["state"].detach().clone()
+    with pytest.raises(ValueError, match="no derivatives"):
+        hip.delta_rule_step(**asks)
+    assert torch.equal(asks["state"], before)
+    with torch.no_grad():
+        assert torch.equal(hip.delta_rule_step(**asks), want)
