@@ -22,6 +22,7 @@ from typing import Optional, Tuple
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import SLA_BF16, SLA_F16, SLA_F32, SLA_OK, SlaError, _on, _raw_stream, load
 
@@ -270,7 +271,7 @@ def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: tor
     float32, contiguous: a pool, of which sequence b owns state[slots[b]]
     (slots int32, all different; without them state[b]).  A slot outside the
     pool marks a place with no request: its o is 0.  Any gate is taken as the
-    formulas stand.  It has no derivatives and refuses tensors that ask for them
+    formulas stand.  Autograd sees the update as one in place.  It has no derivatives and refuses tensors that ask for them
     (under ``torch.no_grad()`` none does)."""
     device = _check_rule(q, k, v, beta, gate, None, None, 1)
     vs, dk = v.shape, q.shape[-1]
@@ -296,4 +297,5 @@ def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: tor
                             slots, o, _stride(o, False), _raw_stream(v))
     if st != SLA_OK:
         raise SlaError(st, "sla_delta_step")
+    increment_version((state, o))
     return o

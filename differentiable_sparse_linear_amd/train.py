@@ -3,7 +3,8 @@ by it, and the AdamW step with the clipping folded in.
 
 Each call goes over the whole list in a few launches (the norm's pass and the
 updating pass), whatever the number and sizes of the tensors, and returns
-without reading anything back to the host.  ``AdamW`` is an optimizer over
+without reading anything back to the host.  Autograd sees what is updated as
+changed in place, as by torch's optimizers.  ``AdamW`` is an optimizer over
 ``adamw_step_``.
 """
 from __future__ import annotations
@@ -13,6 +14,7 @@ import struct
 from typing import Iterable, List, Optional, Sequence
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import SLA_BF16, SLA_F16, SLA_F32, SLA_F64, SLA_OK, SlaError, _on, _ptr, _raw_stream, load
 
@@ -142,6 +144,7 @@ def clip_grad_norm_(grads: Iterable[torch.Tensor], max_norm: float, stream=None)
         st = sla_clip_grads(table, len(grads), max_norm, norm, work, _raw_stream(norm))
     if st != SLA_OK:
         raise SlaError(st, "sla_clip_grads")
+    increment_version(grads)
     return norm
 
 
@@ -199,6 +202,7 @@ def adamw_step_(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
         st = sla_adamw(table, n, opts, norm, work, _raw_stream(params[0]))
     if st != SLA_OK:
         raise SlaError(st, "sla_adamw")
+    increment_version([*params, *exp_avgs, *exp_avg_sqs, *(w for w in masters if w is not None)])
     return norm
 
 

@@ -88,3 +88,43 @@ def test_step_refuses_inputs_that_ask_for_gradients(hip, name):
     assert torch.equal(asks["state"], before)
     with torch.no_grad():
         assert torch.equal(hip.delta_rule_step(**asks), want)
+
+
+# ------------------------------------------- updates in place, as autograd sees them
+
+@pytest.mark.gpu
+def test_backward_across_an_optimizer_step_is_an_error(hip):
+    """A graph that was kept across a step holds weights that are no longer there."""
+    w = torch.nn.Parameter(torch.randn(8, 8, device=DEV))
+    x = torch.randn(4, 8, device=DEV, requires_grad=True)
+    opt = hip.AdamW([w], max_norm=1.0)
+    loss = (x @ w).square().sum()
+    loss.backward(retain_graph=True)
+    opt.step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    opt.zero_grad()
+    (x @ w).square().sum().backward()       # a new graph is as good as ever
+    opt.step()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["clip", "param", "moments", "master", "state", "out"])
+def test_updates_raise_versions(hip, what):
+    f = lambda *s, t=torch.float32: torch.ones(s, device=DEV, dtype=t)
+    if what == "clip":
+        xs = [f(5), f(3, t=torch.float64)]
+        hip.clip_grad_norm_(xs, 1.0)
+    elif what in ("param", "moments", "master"):
+        p, g, m, v, w = [f(5, t=torch.bfloat16)], [f(5, t=torch.bfloat16)], [f(5)], [f(5)], [f(5)]
+        seen = [x._version for x in g]
+        hip.adamw_step_(p, g, m, v, 1, max_norm=1.0, masters=w)
+        xs = {"param": p, "moments": m + v, "master": w}[what]
+        assert [x._version for x in g] == seen      # gradients stay as they are
+    else:
+        c = rule_inputs(DEV)
+        one = {n: x[:, 0].contiguous() if n != "state" else x.clone() for n, x in c.items()}
+        out = torch.empty_like(one["v"])
+        hip.delta_rule_step(**one, out=out)
+        xs = [one["state"] if what == "state" else out]
+    assert all(x._version == 1 for x in xs)
