@@ -47,8 +47,8 @@ struct GradEntry {
 };
 struct AdamEntry {
     void *grad, *param, *exp_avg, *exp_avg_sq, *master;
-    int64_t n;
-    double rate, root;  // lr / (1 - b1^step), 1 / sqrt(1 - b2^step)
+    int64_t n, step, *skipped;
+    double rate, root;  // lr / (1 - b1^step), 1 / sqrt(1 - b2^step), with no step skipped
     int32_t first;
     uint8_t grad_type, param_type, vec;
 };
@@ -278,16 +278,31 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(Table<GradEntry> tb, con
 }
 
 struct AdamArgs {
-    double b1, b2, eps, keep, max_norm;  // keep = 1 - lr weight_decay
+    double lr, b1, b2, eps, keep, max_norm;  // keep = 1 - lr weight_decay
 };
+
+// b^n, n >= 1, by squaring.
+__device__ inline double power(double b, int64_t n) {
+    double y = 1.0;
+    for (; n > 0; n >>= 1, b *= b)
+        if (n & 1) y *= b;
+    return y;
+}
 
 // P the params' type, M the master's (P: there is none), G the gradients'.
 template <typename P, typename M, typename G>
 __device__ void adamw(const AdamEntry &t, int64_t b, int64_t z, const AdamArgs &o,
                       double factor) {
     using W = Wide<M>;
+    double step_rate = t.rate, step_root = t.root;
+    const int64_t skipped = t.skipped ? *t.skipped : 0;
+    if (skipped != 0) {
+        const int64_t step = t.step - skipped > 1 ? t.step - skipped : 1;
+        step_rate = o.lr / (1.0 - power(o.b1, step));
+        step_root = 1.0 / sqrt(1.0 - power(o.b2, step));
+    }
     const W b1 = (W)o.b1, b2 = (W)o.b2, n1 = (W)(1.0 - o.b1), n2 = (W)(1.0 - o.b2),
-            eps = (W)o.eps, keep = (W)o.keep, rate = (W)t.rate, root = (W)t.root, c = (W)factor;
+            eps = (W)o.eps, keep = (W)o.keep, rate = (W)step_rate, root = (W)step_root, c = (W)factor;
     const bool vec = t.vec;
     P *p = static_cast<P *>(t.param);
     M *master = static_cast<M *>(std::is_same_v<P, M> ? t.param : t.master);
@@ -344,7 +359,12 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table<AdamEntry> tb, co
     if (o.max_norm > 0.0) {
         const double norm = norm_of(part, n);
         if (out && blockIdx.x == 0 && threadIdx.x == 0) put_norm(out, type, norm);
-        if (!isfinite(norm)) return;
+        if (!isfinite(norm)) {  // counted by whoever has a tensor's first chunk
+            for_pieces(tb, [&](const AdamEntry &t, int64_t b, int64_t) {
+                if (b == 0 && t.skipped && threadIdx.x == 0) ++*t.skipped;
+            });
+            return;
+        }
         c = clip_factor(norm, o.max_norm);
     }
     for_pieces(tb, [&](const AdamEntry &t, int64_t b, int64_t z) {
@@ -517,7 +537,7 @@ sla_status sla_adamw(const sla_tensor *tensors, int64_t count, const sla_adamw_o
     if (clip && (!d_norm || !norm_type_ok(norm_type) || (count > 0 && !d_work))) return SLA_ERR_ARG;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     AdamArgs o;
-    o.b1 = q.beta_one, o.b2 = q.beta_two, o.eps = q.eps;
+    o.lr = q.lr, o.b1 = q.beta_one, o.b2 = q.beta_two, o.eps = q.eps;
     o.keep = 1.0 - q.lr * q.weight_decay;
     o.max_norm = q.max_norm;
     const double *part = nullptr;
@@ -538,7 +558,7 @@ sla_status sla_adamw(const sla_tensor *tensors, int64_t count, const sla_adamw_o
         x.param = t.param, x.exp_avg = t.exp_avg, x.exp_avg_sq = t.exp_avg_sq;
         x.master = t.master;
         x.param_type = (uint8_t)t.param_type;
-        x.rate = rate, x.root = root;
+        x.rate = rate, x.root = root, x.step = step, x.skipped = t.d_skipped;
         x.vec = aligned(t.grad) && aligned(t.param) && aligned(t.exp_avg) &&
                 aligned(t.exp_avg_sq) && aligned(t.master);
     };

@@ -30,11 +30,11 @@ class _Tensor(ctypes.Structure):
                 ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
                 ("master", ctypes.c_void_p), ("n", ctypes.c_int64),
                 ("step", ctypes.c_int64), ("grad_type", ctypes.c_int32),
-                ("param_type", ctypes.c_int32)]
+                ("param_type", ctypes.c_int32), ("d_skipped", ctypes.c_void_p)]
 
 
 # the structure as struct's native layout packs it
-_PACK = struct.Struct("@5Pqqii")
+_PACK = struct.Struct("@5PqqiiP")
 
 
 class _AdamOpts(ctypes.Structure):
@@ -95,7 +95,7 @@ def _table(rows) -> ctypes.Array:
 
 def _grads_table(grads: Sequence[torch.Tensor], device: int) -> ctypes.Array:
     kinds = _types(grads, "a gradient")
-    return _table((g, 0, 0, 0, 0, x.numel(), 1, kind, kind)
+    return _table((g, 0, 0, 0, 0, x.numel(), 1, kind, kind, 0)
                   for g, x, kind in zip(_addresses(grads, "gradients", device), grads, kinds))
 
 
@@ -152,17 +152,21 @@ def adamw_step_(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                 exp_avgs: Sequence[torch.Tensor], exp_avg_sqs: Sequence[torch.Tensor], step,
                 lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                 weight_decay: float = 1e-2, max_norm: Optional[float] = None,
-                masters: Optional[Sequence[Optional[torch.Tensor]]] = None, stream=None):
+                masters: Optional[Sequence[Optional[torch.Tensor]]] = None, stream=None,
+                skipped: Optional[Sequence[Optional[torch.Tensor]]] = None):
     """One AdamW step (decoupled weight decay) on every tensor, in place.
 
-    ``step`` counts from 1: one number, or one for each tensor.  Moments are float64 for float64 params, else
-    float32; float16 and bfloat16 params may have a float32 master each
-    (``masters``, None where there is none), which the step then updates and
-    the param is the rounding of.  Gradients have the param's type, or
-    float32; float32 params also take float16 and bfloat16 ones.  With
-    ``max_norm`` the gradients are clipped to that global norm as they are
-    read (they stay as they are) and the norm is returned; a norm that is not
-    finite leaves everything as it is."""
+    ``step`` counts from 1: one number, or one for each tensor.  Moments are
+    float64 for float64 params, else float32; float16 and bfloat16 params may
+    have a float32 master each (``masters``, None where there is none), which
+    the step then updates and the param is the rounding of.  Gradients have the
+    param's type, or float32; float32 params also take float16 and bfloat16
+    ones.  With ``max_norm`` the gradients are clipped to that global norm as
+    they are read (they stay as they are) and the norm is returned; a norm that
+    is not finite leaves everything as it is.  ``skipped`` counts such steps
+    where the host does not see them: for each tensor an int64 scalar on the
+    device (or None), raised by one when a step is skipped, and what it holds is
+    taken off the tensor's ``step``."""
     n = len(params)
     masters = [None] * n if masters is None else masters
     steps = [step] * n if isinstance(step, int) else list(step)
@@ -188,13 +192,19 @@ def adamw_step_(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
         if w is not None and (pd in (torch.float32, torch.float64) or w.dtype != torch.float32 or
                               w.numel() != n_g):
             raise ValueError("a master is the float32 copy of a float16 or bfloat16 param")
+    skipped = [None] * n if skipped is None else skipped
+    counters = [x for x in skipped if x is not None]
+    if len(skipped) != n or any(x.dtype != torch.int64 or x.numel() != 1 for x in counters):
+        raise ValueError("skipped must hold an int64 scalar (or None) for each param")
     held = iter(_addresses([w for w in masters if w is not None], "masters", device))
+    counters = iter(_addresses(counters, "counters", device))
     table = _table(zip(_addresses(grads, "gradients", device),
                        _addresses(params, "params", device),
                        _addresses(exp_avgs, "moments", device),
                        _addresses(exp_avg_sqs, "moments", device),
                        [0 if w is None else next(held) for w in masters], sizes, steps,
-                       grad_kinds, kinds))
+                       grad_kinds, kinds,
+                       [0 if x is None else next(counters) for x in skipped]))
     with _on(device, stream):
         norm, work = _norm_and_work(grads, params[0].device) if max_norm is not None \
             else (None, None)
@@ -209,8 +219,11 @@ def adamw_step_(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
 class AdamW(torch.optim.Optimizer):
     """AdamW over ``adamw_step_``: one norm pass and one updating pass for all
     parameters of a group.  ``max_norm`` clips each group's gradients to that
-    global norm within the step (``last_norm`` of the group holds it, on the
-    device); float16 and bfloat16 parameters get float32 masters."""
+    norm within the step, every group by itself (``last_norm`` of the group holds
+    its norm, on the device), and a step whose norm is not finite is skipped and
+    does not count for the bias correction.  float16 and bfloat16 parameters get
+    float32 masters.  Steps are counted on the host: a graph cannot capture them
+    (``adamw_step_`` with a given step it can)."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 1e-2, max_norm: Optional[float] = None):
@@ -225,6 +238,8 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("AdamW.step counts steps on the host: it cannot be captured")
         for group in self.param_groups:
             params = [p for p in group["params"] if p.grad is not None]
             for p in params:
@@ -237,15 +252,19 @@ class AdamW(torch.optim.Optimizer):
                     state["exp_avg_sq"] = torch.zeros_like(state["exp_avg"])
                     state["master"] = p.detach().float() if p.dtype in (
                         torch.float16, torch.bfloat16) else None
-                state["step"] += 1
+                if group["max_norm"] is not None and state.get("skipped") is None:
+                    state["skipped"] = torch.zeros((), dtype=torch.int64, device=p.device)
             if not params:
                 continue
             get = lambda name: [self.state[p][name] for p in params]
             group["last_norm"] = adamw_step_(
-                params, [p.grad for p in params], get("exp_avg"), get("exp_avg_sq"), get("step"),
-                lr=group["lr"], betas=group["betas"], eps=group["eps"],
-                weight_decay=group["weight_decay"], max_norm=group["max_norm"],
-                masters=get("master"))
+                params, [p.grad for p in params], get("exp_avg"), get("exp_avg_sq"),
+                [n + 1 for n in get("step")], lr=group["lr"], betas=group["betas"],
+                eps=group["eps"], weight_decay=group["weight_decay"],
+                max_norm=group["max_norm"], masters=get("master"),
+                skipped=[self.state[p].get("skipped") for p in params])
+            for p in params:
+                self.state[p]["step"] += 1
         return loss
 
     def load_state_dict(self, state_dict):

@@ -445,6 +445,7 @@ typedef struct {
     int64_t n;
     int64_t step;        /* the tensor's AdamW steps, 1 for the first */
     int32_t grad_type, param_type;
+    int64_t *d_skipped;  /* device counter of those steps that were skipped, or NULL */
 } sla_tensor;
 
 /* Device bytes that the three calls below work in. */
@@ -480,7 +481,10 @@ typedef struct {
  * SLA_F64), else fp32 (gradients SLA_F32 or the params' type; for SLA_F32
  * params also SLA_F16 and SLA_BF16).  With a master the step is the master's
  * and param its rounding.  With max_norm > 0, *d_norm gets the norm, and where
- * it is not finite nothing else is written: the step is skipped.
+ * it is not finite the step is skipped: nothing else is written but the
+ * counters d_skipped, which go up by one.  Where a tensor has a counter, `step`
+ * in the formula is the tensor's step less what the counter holds (an empty
+ * tensor's counter stays as it is).
  */
 sla_status sla_adamw(const sla_tensor *tensors, int64_t count, const sla_adamw_opts *opts,
                      void *d_norm, int32_t norm_type, void *d_work, void *stream);
