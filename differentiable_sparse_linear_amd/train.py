@@ -267,6 +267,13 @@ class AdamW(torch.optim.Optimizer):
                 self.state[p]["step"] += 1
         return loss
 
+    def state_dict(self):
+        """Without the groups' ``last_norm``, which is an answer and no state."""
+        saved = super().state_dict()
+        for group in saved["param_groups"]:
+            group.pop("last_norm", None)
+        return saved
+
     def load_state_dict(self, state_dict):
         """Moments and masters keep their own types (the base class casts
         them to the parameters')."""

@@ -122,3 +122,19 @@ def test_counters_are_checked(hip):
             step(bad)
     step([None])
     step([torch.zeros((), device=DEV, dtype=torch.int64)])
+
+
+def test_state_dict_holds_no_answers(hip):
+    """The norm stays with the optimizer; what is saved is numbers and the tensors
+    of the state, and the optimizer that saved goes on as it was."""
+    ps = params(torch.float32)
+    opt = hip.AdamW(ps, max_norm=3.0)
+    put_grads(ps, 0)
+    opt.step()
+    norm = opt.param_groups[0]["last_norm"]
+    saved = opt.state_dict()
+    assert not any(isinstance(x, torch.Tensor) for g in saved["param_groups"] for x in g.values())
+    assert opt.param_groups[0]["last_norm"] is norm
+    other = hip.AdamW(params(torch.float32), max_norm=1.0)
+    other.load_state_dict(saved)
+    assert other.param_groups[0]["max_norm"] == 3.0 and "last_norm" not in other.param_groups[0]
