@@ -106,8 +106,7 @@ Work layout(const DeltaArgs &a, int dtype, bool back) {
 }
 
 int64_t saved_state_bytes(const DeltaArgs &a) {
-    return align256((int64_t)a.B * a.Hv * (num_chunks(a) + 1) * padded_dk(a.dk) *
-                    padded_dv(a.dv) * 4);
+    return align256((int64_t)a.B * a.Hv * num_chunks(a) * padded_dk(a.dk) * padded_dv(a.dv) * 4);
 }
 
 }  // namespace
@@ -187,7 +186,8 @@ sla_status sla_delta_backward(const sla_delta_args *args, const void *d_saved,
         return SLA_ERR_ARG;
     if (d_dstate && d_dstate == d_grad_state) return SLA_ERR_ARG;
     if (args->batch == 0) return SLA_OK;
-    if (!d_saved || (args->tokens > 0 && (!d_grad_o || !d_dq || !d_dk || !d_dv || !d_dbeta || !d_dgate)))
+    if (args->tokens > 0 &&
+        (!d_saved || !d_grad_o || !d_dq || !d_dk || !d_dv || !d_dbeta || !d_dgate))
         return SLA_ERR_ARG;
     const DeltaArgs a = args_of(args);
     const int dtype = args->dtype;

@@ -22,14 +22,11 @@ __host__ __device__ inline int num_chunks(const DeltaArgs &a) {
 }
 __host__ __device__ inline int padded_dv(int dv) { return (dv + 31) / 32 * 32; }
 
-// A training pass keeps the state at every chunk's start and after the last
-// chunk, and W, as the scans hold them: for each chunk and slice of 16 columns
-// the accumulator tiles (of DK / 16 and of 4 row tiles), 4 rows a lane.  The
-// backward scan leaves dS and dR so.
+// A training pass keeps the state at every chunk's start, and W, as the scans
+// hold them: for each chunk and slice of 16 columns the accumulator tiles (of
+// DK / 16 and of 4 row tiles), 4 rows a lane.  The backward scan leaves dS and
+// dR so.
 __host__ __device__ inline int64_t saved_chunk(const DeltaArgs &a, int b, int h) {
-    return ((int64_t)b * a.Hv + h) * (num_chunks(a) + 1);
-}
-__host__ __device__ inline int64_t saved_chunk_w(const DeltaArgs &a, int b, int h) {
     return ((int64_t)b * a.Hv + h) * num_chunks(a);
 }
 

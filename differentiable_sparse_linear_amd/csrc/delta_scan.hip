@@ -334,12 +334,11 @@ delta_scan_kernel(DeltaArgs a, ChunkRange cr, const unsigned char *ws_key,
             for (int m = 0; m < NC; ++m) {
                 if (col0 + 16 * m >= dvp) break;
                 const Buffer dst = buffer(
-                    save_w + ((saved_chunk_w(a, b, h) + n) * dvp + col0 + 16 * m) * kChunk,
+                    save_w + ((saved_chunk(a, b, h) + n) * dvp + col0 + 16 * m) * kChunk,
                     kChunk * kSlice * 4);
                 store16_later(__builtin_bit_cast(u32x4, W[m]), dst, lane16 + 1024 * w, 0);
             }
         key0 = key1, head0 = head1;
-        if (SAVE && (n + 1) * kChunk >= len) keep(n + 1);
     }
     if (s_out)
 #pragma unroll

@@ -128,3 +128,19 @@ def test_updates_raise_versions(hip, what):
         hip.delta_rule_step(**one, out=out)
         xs = [one["state"] if what == "state" else out]
     assert all(x._version == 1 for x in xs)
+
+
+# ------------------------------------------------------ what a training pass keeps
+
+@pytest.mark.parametrize("T,dk,dv", [(0, 64, 64), (1, 64, 64), (64, 128, 32), (65, 20, 33)])
+def test_what_a_training_pass_keeps(T, dk, dv):
+    """A state and 64 rows of W for each chunk and head, padded to whole tiles; no
+    more than that (the state after the last chunk is an output)."""
+    import ctypes
+    import differentiable_sparse_linear_amd as sla
+    from differentiable_sparse_linear_amd import delta as D
+    s = D._Stride(1, 1, 1)
+    args = D._Args(3, T, 1, 2, dk, dv, sla.SLA_F32, 1.0, 16, 16, 16, 16, 16, s, s, s, s, s, None)
+    chunks = -(-T // 64)
+    want = 3 * 2 * chunks * 4 * ((64 if dk <= 64 else 128) + 64) * (-(-dv // 32) * 32)
+    assert sla.load().sla_delta_saved_bytes(ctypes.byref(args)) == want
