@@ -35,8 +35,9 @@ bool valid(const sla_delta_args *p) {
            (p->dtype == SLA_F32 || p->dtype == SLA_F16 || p->dtype == SLA_BF16);
 }
 
-bool has_data(const sla_delta_args *p) {
-    return p->batch * p->tokens == 0 || (p->d_q && p->d_k && p->d_v && p->d_beta && p->d_gate);
+bool has_data(const sla_delta_args *p, bool back = false) {
+    return p->batch * p->tokens == 0 ||
+           (p->d_q && p->d_k && (p->d_v || back) && p->d_beta && p->d_gate);
 }
 
 // The scans address a chunk's rows of v and o in 32 bits and tell a row past
@@ -182,7 +183,7 @@ sla_status sla_delta_backward(const sla_delta_args *args, const void *d_saved,
                               const float *d_grad_state, void *d_dq, void *d_dk, void *d_dv,
                               float *d_dbeta, float *d_dgate, float *d_dstate, void *d_work,
                               int64_t work_bytes, void *stream) {
-    if (!valid(args) || !has_data(args) || !o_stride || !valid_rows(args, o_stride))
+    if (!valid(args) || !has_data(args, true) || !o_stride || !valid_rows(args, o_stride))
         return SLA_ERR_ARG;
     if (d_dstate && d_dstate == d_grad_state) return SLA_ERR_ARG;
     if (args->batch == 0) return SLA_OK;

@@ -194,8 +194,8 @@ def _forward(q, k, v, beta, gate, state, scale, lengths, save: bool):
 
 class DeltaRule(torch.autograd.Function):
     """(o, last state) of ``delta_rule``'s arguments, checked as there; saves
-    the inputs, the state at every chunk's start and W (4 (dk / 64 + 1) dv bytes
-    a token and value head, dk and dv padded to whole tiles)."""
+    the inputs but v, the state at every chunk's start and W (4 (dk / 64 + 1) dv
+    bytes a token and value head, dk and dv padded to whole tiles)."""
 
     @staticmethod
     def forward(ctx, q, k, v, beta, gate, state, scale, lengths):
@@ -205,26 +205,27 @@ class DeltaRule(torch.autograd.Function):
             o, last, saved = _forward(q, k, v, beta, gate, state, scale, lengths,
                                       any(ctx.needs_input_grad))
         if saved is not None:
-            ctx.save_for_backward(q, k, v, beta, gate, lengths, saved)
-            ctx.scale, ctx.has_state = scale, state is not None
+            ctx.save_for_backward(q, k, beta, gate, lengths, saved)
+            ctx.scale, ctx.has_state, ctx.dv = scale, state is not None, v.shape[3]
             ctx.set_materialize_grads(False)
         return o, last
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_o, grad_last):
-        q, k, v, beta, gate, lengths, saved = ctx.saved_tensors
-        args = _make_args(q, k, v, beta, gate, ctx.scale, lengths)
-        grad_o = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if grad_o is None \
-            else _rows(grad_o, tokens=True)
-        grad_last = None if grad_last is None else grad_last.contiguous()
+        q, k, beta, gate, lengths, saved = ctx.saved_tensors
         new = lambda x: torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dq, dk, dv, dbeta, dgate = new(q), new(k), new(v), new(beta), new(gate)
-        dstate = torch.empty((v.shape[0], v.shape[2], q.shape[3], v.shape[3]),
-                             device=v.device) if ctx.has_state else None
-        work = _bytes(sla_delta_workspace_bytes(args, backward=True), v.device)
+        dq, dk, dbeta, dgate = new(q), new(k), new(beta), new(gate)
+        dv = torch.empty((*beta.shape, ctx.dv), dtype=q.dtype, device=q.device)
+        grad_o = torch.zeros_like(dv) if grad_o is None else _rows(grad_o, tokens=True)
+        grad_last = None if grad_last is None else grad_last.contiguous()
+        dstate = torch.empty((q.shape[0], beta.shape[2], q.shape[3], ctx.dv),
+                             device=q.device) if ctx.has_state else None
+        # dv in v's place: of the shape and type, and not read
+        args = _make_args(q, k, dv, beta, gate, ctx.scale, lengths)
+        work = _bytes(sla_delta_workspace_bytes(args, backward=True), q.device)
         st = sla_delta_backward(args, saved, grad_o, _stride(grad_o), grad_last, dq, dk, dv,
-                                dbeta, dgate, dstate, work, _raw_stream(v))
+                                dbeta, dgate, dstate, work, _raw_stream(q))
         if st != SLA_OK:
             raise SlaError(st, "sla_delta_backward")
         return dq, dk, dv, dbeta, dgate, dstate, None, None

@@ -413,7 +413,7 @@ sla_status sla_delta_forward(const sla_delta_args *args, const float *d_state_in
 /*
  * sla_delta_backward -- gradients for the upstream d_grad_o (strides as o's)
  * and d_grad_state (of the last state; NULL: zero), from what the forward pass
- * with the same arguments saved.  Writes d_dq, d_dk [batch][tokens][key_heads][dk]
+ * with the same arguments saved (v is not read: d_v may be NULL).  Writes d_dq, d_dk [batch][tokens][key_heads][dk]
  * and d_dv [batch][tokens][value_heads][dv] (type dtype, contiguous; a shared
  * head's gradient is the sum over the value heads that read it), d_dbeta and
  * d_dgate [batch][tokens][value_heads] (fp32, contiguous) and, unless NULL,

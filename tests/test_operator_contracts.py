@@ -144,3 +144,50 @@ def test_what_a_training_pass_keeps(T, dk, dv):
     chunks = -(-T // 64)
     want = 3 * 2 * chunks * 4 * ((64 if dk <= 64 else 128) + 64) * (-(-dv // 32) * 32)
     assert sla.load().sla_delta_saved_bytes(ctypes.byref(args)) == want
+
+
+@pytest.mark.gpu
+def test_values_are_free_after_the_forward_pass(hip):
+    """No gradient reads v: it may be written over, and is not held."""
+    import gc
+    import weakref
+    c = rule_inputs(DEV)
+    leaves = {n: x.clone().requires_grad_() for n, x in c.items()}
+    want = torch.autograd.grad(hip.delta_rule(**leaves)[0].square().sum(), list(leaves.values()))
+    v = leaves["v"] * 1.0
+    o = hip.delta_rule(**{**leaves, "v": v})[0]
+    with torch.no_grad():
+        v.fill_(float("nan"))
+    got = torch.autograd.grad(o.square().sum(), list(leaves.values()))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    v = c["v"].clone()
+    kept = dict(leaves, v=v)
+    o = hip.delta_rule(**kept)[0]
+    held = weakref.ref(v)
+    del v, kept
+    gc.collect()
+    assert held() is None
+    o.sum().backward()
+
+
+@pytest.mark.gpu
+def test_raw_backward_without_values(hip):
+    from differentiable_sparse_linear_amd import delta as D
+    c = rule_inputs(DEV)
+    q, k, v, beta, gate, state = c.values()
+    o, last, saved = D._forward(q, k, v, beta, gate, state, 1.0, None, True)
+
+    def back(args):
+        out = [torch.empty_like(x) for x in (q, k, v, beta, gate)]
+        work = D._bytes(D.sla_delta_workspace_bytes(args, backward=True), DEV)
+        st = D.sla_delta_backward(args, saved, torch.ones_like(v), D._stride(v), None, *out, None,
+                                  work, 0)
+        return st, out
+
+    torch.cuda.synchronize()
+    args = D._make_args(q, k, v, beta, gate, 1.0, None)
+    st, want = back(args)
+    args.d_v = None
+    other, got = back(args)
+    torch.cuda.synchronize()
+    assert st == other == hip.SLA_OK and all(torch.equal(a, b) for a, b in zip(got, want))
