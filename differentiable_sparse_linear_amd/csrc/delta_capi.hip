@@ -9,12 +9,21 @@ namespace sla {
 namespace {
 
 // Without a backward pass to follow, few tokens are walked by the recurrent
-// kernel, whose time grows with them: 1.8 us a token up to 128 heads and 2.3 with
-// 512 (of 128 x 128, bf16).  A single chunk takes 12.6 us with 16 heads, 22 with
-// 128 and 67 with 512, so the two meet at 4, 9 and 25 tokens (8 tokens: 19.3
-// against 12.6 us, 20.5 against 22.4, 28.5 against 66.5).
-bool few_tokens(const DeltaArgs &a) {
-    const int64_t most = 4 + (int64_t)a.B * a.Hv / 24;
+// kernel, whose time grows with them, where one chunk's hardly does, but with the
+// states' size and the inputs' planes.  Tokens at which the two meet (GPU time; in
+// brackets us for 8 tokens, walked and as a chunk):
+//
+//   heads                  16               128               512
+//   128 x 128, bf16    7.1 (15.1, 13.2)  12 (18.0, 24.3)   28 (29.8, 72.7)
+//    64 x  64, bf16    6.6 (13.4, 11.3)   8 (13.9, 13.7)   17 (18.6, 32.7)
+//    32 x  32, bf16    6.5 (13.2, 11.2)   7 (13.4, 12.1)   11 (17.1, 21.6)
+//   128 x 128, fp32    12  (12.8, 17.5)  20 (16.0, 31.7)   58 (26.7, 119)
+//    64 x  64, fp32    9.3 (12.0, 13.4)  12 (12.3, 16.6)   28 (17.2, 44.5)
+//    32 x  32, fp32    9.2 (11.8, 13.3)  11 (12.0, 14.6)   19 (15.6, 30.2)
+bool few_tokens(const DeltaArgs &a, int dtype) {
+    const int planes = dtype == SLA_F32 ? 3 : dtype == SLA_F16 ? 2 : 1;
+    const double states = (double)a.B * a.Hv * a.dk * a.dv / (kMaxDk * kMaxDk);
+    const double most = 4.5 + 1.5 * planes + states * (planes + 1) / 40;
     return a.T <= (most < 24 ? most : 24);
 }
 
@@ -150,7 +159,7 @@ sla_status sla_delta_forward(const sla_delta_args *args, const float *d_state_in
     const DeltaArgs a = args_of(args);
     const int dtype = args->dtype;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    if (!d_saved && few_tokens(a)) {
+    if (!d_saved && few_tokens(a, dtype)) {
         DELTA_TRY(launch_delta_step(dtype, a, d_state_in, d_state_out, nullptr, 0, d_o, o_stride[0],
                                     o_stride[1], o_stride[2], kMaxGrowth, s));
         return SLA_OK;
