@@ -279,6 +279,7 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(Table<GradEntry> tb, con
 
 struct AdamArgs {
     double lr, b1, b2, eps, keep, max_norm;  // keep = 1 - lr weight_decay
+    double rate, root;                       // of the tensor at hand
 };
 
 // b^n, n >= 1, by squaring.
@@ -289,20 +290,32 @@ __device__ inline double power(double b, int64_t n) {
     return y;
 }
 
+// A value that is the same in all lanes, in scalar registers.
+__device__ inline double uniform(double x) {
+    const uint64_t y = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)y),
+                   hi = __builtin_amdgcn_readfirstlane((uint32_t)(y >> 32));
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// The tensor's rate and root: the host's where no step was skipped (134M bf16
+// values with masters: 206 us a launch of three; from then on 225).
+__device__ inline void set_rates(const AdamEntry &t, AdamArgs &o) {
+    o.rate = t.rate, o.root = t.root;
+    const int64_t skipped = t.skipped ? *t.skipped : 0;
+    if (skipped == 0) return;
+    const int64_t step = t.step - skipped > 1 ? t.step - skipped : 1;
+    o.rate = uniform(o.lr / (1.0 - power(o.b1, step)));
+    o.root = uniform(1.0 / sqrt(1.0 - power(o.b2, step)));
+}
+
 // P the params' type, M the master's (P: there is none), G the gradients'.
 template <typename P, typename M, typename G>
 __device__ void adamw(const AdamEntry &t, int64_t b, int64_t z, const AdamArgs &o,
                       double factor) {
     using W = Wide<M>;
-    double step_rate = t.rate, step_root = t.root;
-    const int64_t skipped = t.skipped ? *t.skipped : 0;
-    if (skipped != 0) {
-        const int64_t step = t.step - skipped > 1 ? t.step - skipped : 1;
-        step_rate = o.lr / (1.0 - power(o.b1, step));
-        step_root = 1.0 / sqrt(1.0 - power(o.b2, step));
-    }
     const W b1 = (W)o.b1, b2 = (W)o.b2, n1 = (W)(1.0 - o.b1), n2 = (W)(1.0 - o.b2),
-            eps = (W)o.eps, keep = (W)o.keep, rate = (W)step_rate, root = (W)step_root, c = (W)factor;
+            eps = (W)o.eps, keep = (W)o.keep, rate = (W)o.rate, root = (W)o.root, c = (W)factor;
     const bool vec = t.vec;
     P *p = static_cast<P *>(t.param);
     M *master = static_cast<M *>(std::is_same_v<P, M> ? t.param : t.master);
@@ -368,6 +381,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table<AdamEntry> tb, co
         c = clip_factor(norm, o.max_norm);
     }
     for_pieces(tb, [&](const AdamEntry &t, int64_t b, int64_t z) {
+        set_rates(t, o);
         switch (t.param_type) {
             case SLA_F64: adamw<double, double, double>(t, b, z, o, c); break;
             case SLA_F32:
