@@ -25,9 +25,11 @@ __host__ __device__ inline int padded_dv(int dv) { return (dv + 31) / 32 * 32; }
 // A training pass keeps the state at every chunk's start, and W, as the scans
 // hold them: for each chunk and slice of 16 columns the accumulator tiles (of
 // DK / 16 and of 4 row tiles), 4 rows a lane.  The backward scan leaves dS and
-// dR so.
-__host__ __device__ inline int64_t saved_chunk(const DeltaArgs &a, int b, int h) {
-    return ((int64_t)b * a.Hv + h) * num_chunks(a);
+// dR so.  All heads' parts of a chunk stand together: the scans write them at about
+// the same time, and with a head's chunks together they would be whole powers
+// of 2 apart.
+__host__ __device__ inline int64_t saved_chunk(const DeltaArgs &a, int b, int h, int n) {
+    return ((int64_t)n * a.B + b) * a.Hv + h;
 }
 
 // Whether the rows of q and k can be read four elements at a time.

@@ -93,10 +93,10 @@ delta_grad_kernel(DeltaArgs a, ChunkRange cr, bool vec_q, bool vec_o, const unsi
         const int h = hk * group + m;
         const int64_t at = cr.chunk(a, b, h, blockIdx.x);
         const uint32_t state_bytes = DK * dvp * 4, row_bytes = kChunk * dvp * 4;
-        const Buffer S = buffer(save_s + (saved_chunk(a, b, h) + n) * DK * dvp, state_bytes),
+        const Buffer S = buffer(save_s + saved_chunk(a, b, h, n) * DK * dvp, state_bytes),
                      dS = buffer(ws_ds + at * DK * dvp, state_bytes),
                      rows = half ? buffer(ws_dr + at * kChunk * dvp, row_bytes)
-                                 : buffer(save_w + (saved_chunk(a, b, h) + n) * kChunk * dvp, row_bytes);
+                                 : buffer(save_w + saved_chunk(a, b, h, n) * kChunk * dvp, row_bytes);
         const float *scalars =
             reinterpret_cast<const float *>(ws_head + at * L::kPerHead + 2 * L::kTri);
         const int rows_here = len - t0 < kChunk ? len - t0 : kChunk;

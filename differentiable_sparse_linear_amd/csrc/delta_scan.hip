@@ -218,7 +218,7 @@ delta_scan_kernel(DeltaArgs a, ChunkRange cr, const unsigned char *ws_key,
 #pragma unroll
         for (int m = 0; m < NC; ++m) {
             if (col0 + 16 * m >= dvp) break;
-            const Buffer dst = buffer(save_s + ((saved_chunk(a, b, h) + n) * dvp + col0 + 16 * m) * DK,
+            const Buffer dst = buffer(save_s + (saved_chunk(a, b, h, n) * dvp + col0 + 16 * m) * DK,
                                       DK * kSlice * 4);
 #pragma unroll
             for (int t = 0; t < TW; ++t)
@@ -334,7 +334,7 @@ delta_scan_kernel(DeltaArgs a, ChunkRange cr, const unsigned char *ws_key,
             for (int m = 0; m < NC; ++m) {
                 if (col0 + 16 * m >= dvp) break;
                 const Buffer dst = buffer(
-                    save_w + ((saved_chunk(a, b, h) + n) * dvp + col0 + 16 * m) * kChunk,
+                    save_w + (saved_chunk(a, b, h, n) * dvp + col0 + 16 * m) * kChunk,
                     kChunk * kSlice * 4);
                 store16_later(__builtin_bit_cast(u32x4, W[m]), dst, lane16 + 1024 * w, 0);
             }
