@@ -238,10 +238,12 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("AdamW.step counts steps on the host: it cannot be captured")
         for group in self.param_groups:
             params = [p for p in group["params"] if p.grad is not None]
+            if any(not p.is_cuda for p in params):
+                raise ValueError("params must be device tensors")
+            if params and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("AdamW.step counts steps on the host: it cannot be captured")
             for p in params:
                 state = self.state[p]
                 if not state:

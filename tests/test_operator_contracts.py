@@ -191,3 +191,16 @@ def test_raw_backward_without_values(hip):
     other, got = back(args)
     torch.cuda.synchronize()
     assert st == other == hip.SLA_OK and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------ the optimizer
+
+def test_optimizer_refuses_host_parameters():
+    from differentiable_sparse_linear_amd import AdamW
+    p = torch.nn.Parameter(torch.ones(3))
+    opt = AdamW([p], max_norm=1.0)
+    opt.step()                      # nothing has a gradient
+    p.grad = torch.ones(3)
+    with pytest.raises(ValueError, match="device tensors"):
+        opt.step()
+    assert not opt.state and torch.equal(p.detach(), torch.ones(3))
