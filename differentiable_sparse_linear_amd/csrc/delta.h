@@ -11,8 +11,8 @@
 // its row).  Value head h reads query and key head h / (Hv / Hk).
 //
 // The recurrent kernel (delta_step.hip) walks tokens.  The chunked kernels
-// (delta_chunk.hip, delta_grad.hip) take kChunk tokens at a time, with G_i
-// the chunk's running sum of gates and D_ij = exp(G_i - G_j):
+// (delta_prep.hip, delta_scan.hip, delta_grad.hip) take kChunk tokens at a time,
+// with G_i the chunk's running sum of gates and D_ij = exp(G_i - G_j):
 //
 //   (I + L) W = V - Gamma K S     L_ij = D_ij (k_i . k_j) beta_j,  j < i
 //   O  = scale (Gamma Q S + P' W)  P'_ij = D_ij (q_i . k_j) beta_j, j <= i

@@ -29,8 +29,9 @@ bool few_tokens(const DeltaArgs &a, int dtype) {
 
 // A round's workspace is kept near this, so that what one launch leaves the
 // next one finds in the 256 MB Infinity Cache, and yet a launch is long.  16384
-// tokens of 16 heads of 128 x 128: 482 us, with 80 MB 503 and with 400 MB 553;
-// training on 8192 tokens of 16 heads of 64 x 128: 638, 644 and 674 us.
+// tokens of 16 heads of 128 x 128: 479 us, with 80 MB 511 and with 400 MB 583;
+// training on 8192 tokens of 16 heads of 64 x 128: 648, 683 and 704 us, on 4 x 2048
+// of 128 x 128 560, 617 and 554.
 constexpr int64_t kRoundBytes = 160 << 20;
 
 int64_t align256(int64_t x) { return (x + 255) & ~(int64_t)255; }

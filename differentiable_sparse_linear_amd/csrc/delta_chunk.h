@@ -1,4 +1,5 @@
-// Launches of the chunked gated delta rule (delta_chunk.hip, delta_grad.hip).
+// Launches of the chunked gated delta rule (delta_prep.hip, delta_scan.hip,
+// delta_grad.hip).
 #pragma once
 
 #include "delta_tile.h"

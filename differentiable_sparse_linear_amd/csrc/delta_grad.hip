@@ -32,11 +32,13 @@ namespace {
 // once, staged in LDS 32 value columns at a time and read back transposed; the
 // next columns' tiles are loaded meanwhile.
 //
-// 64 heads of 128 x 128 over 1024 tokens (bf16) take 106 us, 2 TB/s of the 208 KB
-// a chunk and head; 16 heads of 64 x 128 over 4096 tokens 75-80.  Without the
-// loads they take 96 and 75, without the products with S and dS 97 and 76:
-// two wavefronts a SIMD wait in turn for loads, LDS and each other.  Four
-// (1024 threads, 128 registers) spill: 142 and 85.  A double stage: 104 and 83.
+// 64 heads of 128 x 128 over 1024 tokens (bf16) take 124 us, 1.7 TB/s of the 208 KB
+// a chunk and head; 16 heads of 64 x 128 over 4096 tokens 91: two wavefronts a SIMD
+// wait in turn for loads, LDS and each other (48 % of their cycles; matrix
+// instructions busy 16 % of the time).  The pairs' part of the gates' gradient is
+// 16 and 10 us of it; before it was there, four wavefronts a SIMD (1024 threads,
+// 128 registers, which spill) took 142 and 85 us against 106 and 75, a double
+// stage 104 and 83.
 template <typename T, int DK, bool GROUP>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void
 delta_grad_kernel(DeltaArgs a, ChunkRange cr, bool vec_q, bool vec_o, const unsigned char *ws_key,

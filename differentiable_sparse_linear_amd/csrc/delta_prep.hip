@@ -30,10 +30,10 @@ __device__ inline void put16(u32x4 x, unsigned char *to, uint32_t lane16) {
 // four that complete the whole, each [A 0; C B]^-1 = [A^-1 0; -B^-1 C A^-1 B^-1].
 //
 // A workgroup waits on the latency of its loads, barriers and short products
-// for two thirds of its time, so four of them share a CU where the planes
-// allow (128 registers): 112 chunks of 16 heads (bf16) take 56 us with 128 keys,
-// 155 MB written at 2.8 TB/s, and 58 with 256 registers; 128 chunks of 16 heads
-// with 64 keys 39.6 and 44.9.
+// for most of its time, so four of them share a CU where the planes allow (128
+// registers): 112 chunks of 16 heads (bf16) take 50 us with 128 keys, 155 MB
+// written at 3.1 TB/s, and 49 with 256 registers; 128 chunks of 16 heads with 64
+// keys 39.4 and 40.3, for the backward pass 22.4 and 22.9 a launch of 64.
 template <typename T, int DK, bool BWD>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(Planes<T>::n == 1 ? 4 : 2))) void
 delta_prep_kernel(DeltaArgs a, ChunkRange cr, bool vec, unsigned char *ws_key,

@@ -11,10 +11,12 @@
 // the same planes, beside the chain of products that carries the state.
 //
 // Bound by that chain: 1.4 us a chunk with 16 columns (bf16, 128 keys, 16 heads,
-// half of the CUs at work) and 1.2 with all operands at hand; 2.9 with one
-// wavefront a workgroup and nothing exchanged, which alone on a SIMD issues one
-// instruction in four cycles.  64 heads, 32 columns: 2.5 us a chunk, 4.0 with
-// what the gradients need, 96 KB a chunk and head, stored at 1.6 TB/s; back 4.5.
+// half of the CUs at work), 1.6 with 64 keys and what the gradients need; 2.9 with
+// one wavefront a workgroup and nothing exchanged, which alone on a SIMD issues
+// one instruction in four cycles.  64 heads, 32 columns: 2.7 us a chunk, 4.0 with
+// what the gradients need, 96 KB a chunk and head, stored at 1.6 TB/s; back 4.4.
+// The output's products in 24 bits instead of 16 are 0.1 us of a chunk, with 64
+// keys 0.2.
 #include <type_traits>
 
 #include "delta_chunk.h"
@@ -586,10 +588,11 @@ delta_scan_back_kernel(DeltaArgs a, ChunkRange cr, const unsigned char *ws_key,
 }
 
 // 32 columns a workgroup where that still leaves one for every CU: 64 heads of
-// 128 x 128 over 2048 tokens take 81 us against 101 with 16 (bf16), 127 against
-// 150 with what the gradients need, and back 73 against 78; 96 heads of 96 x 112
-// over 1000 tokens 94 against 122 (fp32).  16 heads, which would leave three
-// quarters of the CUs idle, take 170 against 117, back 166 against 100.
+// 128 x 128 over 2048 tokens take 86 us against 108 with 16 (bf16), 119 against
+// 153 with what the gradients need, and back 142 against 148; 96 heads of 96 x 112
+// over 1000 tokens 134 against 153 (fp32).  16 heads, which would leave three
+// quarters of the CUs idle: 281 against 195 (8192 tokens of 128 x 128), training on
+// 64 x 128 298 against 219, back 333 against 196.
 bool two_slices(const DeltaArgs &a, int slices) {
     return (int64_t)a.B * a.Hv * ((slices + 1) / 2) >= 256;
 }

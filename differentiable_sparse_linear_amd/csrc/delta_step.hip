@@ -25,7 +25,7 @@ struct StepArgs {
 //   S_t^T q = a (S^T q) + (q . k) beta w,
 // so a token costs one reduction over the row groups, and one token reads
 // and writes each state once: 8 dk dv bytes a head, which bounds it: 6144 heads
-// of 128 x 128 (bf16 rows) take 156 us, 5.1 TB/s; 16 heads 5.3 us, little more
+// of 128 x 128 (bf16 rows) take 162 us, 5.0 TB/s; 16 heads 5.3 us, little more
 // than a launch.
 template <typename T, int CL, int RPT, int VEC>
 __global__ __launch_bounds__(kThreads) void delta_step_kernel(StepArgs p) {

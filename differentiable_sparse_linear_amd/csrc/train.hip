@@ -11,9 +11,9 @@
 //
 // Every kernel is bound by the bytes it streams (a 4 GiB copy moves 4.75 TB/s
 // on the same card).  200M gradients, bf16 and fp32: the norm reads 402 MB in
-// 88 us (120 us through the caches), clipping reads and writes them in 150 us
-// (246 us with 2048 workgroups that each walk a long run of chunks instead of
-// one workgroup a chunk).  AdamW on 150M parameters, 4.2 GB: 732 us, 5.7 TB/s
+// 88-91 us (120 us through the caches), clipping reads and writes them in 150-168
+// us (246 us with 2048 workgroups that each walk a long run of chunks instead of
+// one workgroup a chunk).  AdamW on 150M parameters, 4.2 GB: 757 us, 5.5 TB/s
 // (1260 us with 2048 workgroups).
 #include <cmath>
 #include <type_traits>
@@ -30,7 +30,8 @@ constexpr int kThreads = 256;
 // 8192, 166 with 4096, 502 with 1024; the norm of 4M in 7 us against 12).  AdamW's
 // workgroups have five arrays each, and one vector of four of each a thread is
 // enough in flight: 150M values in 732 us with 1024, 816 with 4096, 844 with
-// 8192; 64k values in 3.2 us against 7.4.
+// 8192; 64k values in 3.2 us against 7.4 (all without the counters of skipped
+// steps in the table).
 constexpr int kGradElems = 8192, kStepElems = 1024;
 constexpr int kMaxSums = 2048;       // partial sums of one table: 8 workgroups a CU
 constexpr int kMaxBlocks = 1 << 20;  // workgroups of an updating launch
