@@ -366,10 +366,10 @@ enum { SLA_F16 = 2, SLA_BF16 = 3 };                /* tensor types, with SLA_F32
  * _backward) take them in chunks of 64 tokens and allow for growth as long as no
  * run of gates within a chunk sums to more than 2; where one does, or a gate is
  * NaN, the head's answers are NaN from there on, and may be from the chunk's
- * first token.  A q, k, v or beta in use that is not finite makes answers NaN
- * likewise: those of its head (of v: its column) from its chunk on.  Gradients
- * of a head with such a token are NaN.  sla_delta_step takes any gate, token by
- * token as the formulas stand.
+ * first token.  A q, k, v or beta in use that is not finite reaches no more than
+ * that: answers of its head (of v: of its column) from its chunk's first token on
+ * and its head's gradients.  sla_delta_step takes any gate, token by token as the
+ * formulas stand.
  */
 typedef struct {
     int64_t batch, tokens;                   /* sequences; tokens of each (padded) */

@@ -104,3 +104,39 @@ def test_single_tokens_take_any_gate(hip, gate):
                             scale=1.0)
     wo, wS = OD.rule(**c, state=start, scale=1.0)
     assert rel(o, wo[:, 0]) <= 1e-6 and rel(S, wS) <= 1e-6
+
+
+@pytest.mark.parametrize("T", [9, 150])
+@pytest.mark.parametrize("name", ["q", "k", "v", "beta"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_values_that_are_not_finite_stay_in_their_head(hip, T, name, bad):
+    """They show in their token's answer, and reach no other sequence or head, no
+    chunk before theirs, and from v no other column."""
+    c = inputs(T, 34, equal=False)
+    clean, clean_S, clean_g = rule(hip, c, torch.ones_like(c["v"]))
+    at, head = T // 2 + 1, 1 if name in ("v", "beta") else 0
+    c[name] = c[name].clone()
+    if name == "beta":
+        c[name][0, at, head] = bad
+    else:
+        c[name][0, at, head, 3] = bad
+    o, S, grads = rule(hip, c, torch.ones_like(c["v"]))
+    heads = [head] if name in ("v", "beta") else [0, 1]     # two value heads read a key head
+    others = [h for h in range(4) if h not in heads]
+    assert torch.equal(o[1], clean[1]) and torch.equal(S[1], clean_S[1])
+    assert torch.equal(o[0][:, others], clean[0][:, others])
+    assert torch.equal(S[0, others], clean_S[0, others])
+    first = at // 64 * 64
+    assert torch.equal(o[0, :first], clean[0, :first])
+    hit = o[0, at][heads]
+    if name == "v":
+        assert not torch.isfinite(hit[:, 3]).any()
+        rest = [i for i in range(40) if i != 3]
+        assert torch.equal(o[0, :, head][:, rest], clean[0, :, head][:, rest])
+        assert torch.equal(S[0, head][:, rest], clean_S[0, head][:, rest])
+    else:
+        assert not torch.isfinite(hit).any()
+    for n, x, y in zip("qkvbg", grads, clean_g):
+        assert torch.equal(x[1], y[1])
+        if n in "vbg":
+            assert torch.equal(x[0][:, others], y[0][:, others])
